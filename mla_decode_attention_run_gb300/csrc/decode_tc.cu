@@ -1494,7 +1494,9 @@ __device__ void softmax_wg(const DecodeParams& p, const WgCtx& w, const SegView<
                 }
             }
             // P = 2^(s - m) <= 2^kTau, stored as two E4M3 terms of p * kPScale;
-            // its buffer was last read by PV(i - 2)
+            // its buffer was last read by PV(i - 2).  Hidden and missing tokens
+            // (s = -inf) weigh 0, m = -inf or not; a NaN row's s is NaN, which
+            // moves no maximum but makes p and l NaN also while m is -inf.
             if (i >= 2) bwait<G>(&w.bars[PV_DONE + slot], (u & 1) ^ 1, w.abort, w.flags);
             uint32_t pk1[kHL / 4], pk2[kHL / 4];
 #pragma unroll
@@ -1503,8 +1505,8 @@ __device__ void softmax_wg(const DecodeParams& p, const WgCtx& w, const SegView<
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
                     const int j = 4 * e2 + 2 * hh;
-                    const float x0 = m[j] == -INFINITY ? 0.f : fast_exp2(s[j] - m[j]) * kPScale;
-                    const float x1 = m[j + 1] == -INFINITY ? 0.f : fast_exp2(s[j + 1] - m[j + 1]) * kPScale;
+                    const float x0 = s[j] == -INFINITY ? 0.f : fast_exp2(s[j] - m[j]) * kPScale;
+                    const float x1 = s[j + 1] == -INFINITY ? 0.f : fast_exp2(s[j + 1] - m[j + 1]) * kPScale;
                     // x = p1 + p2 / 2^5: p1 the nearest E4M3, p2 the nearest
                     // E4M3 to 2^5 times the remainder, taken in f16 (x <= 256
                     // keeps 11 bits there, f16(x) - p1 is exact and at most 8,
@@ -1538,7 +1540,8 @@ __device__ void softmax_wg(const DecodeParams& p, const WgCtx& w, const SegView<
             if (half_reduce_writer<kHL>(w.lane)) lsum[w.wq * G + w.hb + half_reduce_index<kHL>(w.lane)] = hsum;
         }
         wg_bar(w.wg);
-        // inverse denominators of the warpgroup's heads h0 + t; a head whose q
+        // inverse denominators of the warpgroup's heads h0 + t (0 where no token
+        // was seen, NaN where a NaN row was); a head whose q
         // held an infinity or a NaN has NaN multipliers: its output and lse
         // become NaN (nothing else of it is NaN).  One lane per head, through
         // shared memory, rather than all 16 in every thread (16 divisions of
@@ -1552,14 +1555,14 @@ __device__ void softmax_wg(const DecodeParams& p, const WgCtx& w, const SegView<
             if (w.wq == 0 && w.lane < 16) {
                 const int h = w.h0 + w.lane;
                 const float L = lsum[h] + lsum[G + h] + lsum[2 * G + h] + lsum[3 * G + h];
-                invs[w.lane] = (L > 0.f ? p.k_scale / L : 0.f) + (coef[h] - coef[h]);
+                invs[w.lane] = (L == 0.f ? 0.f : p.k_scale / L) + (coef[h] - coef[h]);
             }
         } else {
 #pragma unroll
             for (int t = 0; t < 16; ++t) {
                 const int h = w.h0 + t;
                 const float L = lsum[h] + lsum[G + h] + lsum[2 * G + h] + lsum[3 * G + h];
-                inv[t] = (L > 0.f ? p.k_scale / L : 0.f) + (coef[h] - coef[h]);
+                inv[t] = (L == 0.f ? 0.f : p.k_scale / L) + (coef[h] - coef[h]);
             }
         }
         // denominators for the lse: 16-head CTAs one per lane (head hb + (lane
