@@ -137,7 +137,9 @@ mla_status_t mla_decode_plan(mla_plan_t* plan, const int32_t* kv_indptr_host,
  *     out[b][h] = sum_t softmax(s)_t * v_t        (BF16)
  *     lse[b][h] = ln sum_t exp(s_t)               (fp32, natural log)
  * A request with seq_len 0 gets out = 0 and lse = -inf; a head whose query
- * row holds an infinity or a NaN gets out = NaN and lse = NaN.
+ * row holds an infinity or a NaN gets out = NaN and lse = NaN, and so do all
+ * heads of a request with a token whose cache row holds a NaN (FP8 and 4-bit
+ * plans).
  * Arithmetic of FP8 plans: the E4M3 cache bytes are the tensor-core operands
  * as they are; each query row enters as three E4M3 terms (exactly for every
  * entry above 2^-14 of the row's largest, with 4 significant bits below) and
@@ -265,7 +267,8 @@ mla_status_t mla_extend_plan(mla_plan_t* plan, const int32_t* qo_indptr_host,
  *     s_t = softmax_scale * sum_d q[n][h][d] * k_t[d],   t <= pos_n
  *     out[n][h] = sum_{t <= pos_n} softmax(s)_t * v_t    (BF16)
  *     lse[n][h] = ln sum_{t <= pos_n} exp(s_t)          (fp32)
- * with k_t, v_t as in mla_decode_run.
+ * with k_t, v_t as in mla_decode_run.  A token whose cache row holds a NaN
+ * makes the rows that see it NaN (out and lse), and no others.
  *  q                BF16, element (n, h, d) at q + n*q_stride_tok +
  *                   h*q_stride_h + d (elements; d < 576 contiguous), n <
  *                   qo_indptr[batch].

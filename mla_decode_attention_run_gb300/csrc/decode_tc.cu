@@ -1427,6 +1427,7 @@ __device__ void softmax_wg(const DecodeParams& p, const WgCtx& w, const SegView<
             // heads h0 + 8 .. h0 + 15 of the same row (term 1 at column h,
             // term 2 at column G + h)
             float s[kHL];
+            [[maybe_unused]] bool nan_row = false;
             {
                 uint32_t r1[kHL], r2[kHL], r3[kHL];
                 const uint32_t sc = w.tmem_lane + kColS + S::kSCols * slot + w.h0;
@@ -1434,6 +1435,9 @@ __device__ void softmax_wg(const DecodeParams& p, const WgCtx& w, const SegView<
                 tmem_ld_half8<kHL>(sc + G, r2);
                 tmem_ld_half8<kHL>(sc + 2 * G, r3);
                 tmem_wait_ld();
+                // the images hold no NaN, so any product with a row is NaN if
+                // the row holds one, and only then
+                if constexpr (E) nan_row = isnan(__uint_as_float(r1[0]));
 #pragma unroll
                 for (int j = 0; j < kHL; ++j)
                     s[j] = valid ? fmaf(__uint_as_float(r1[j]) + __uint_as_float(r2[j]), coef[w.hb + j],
@@ -1443,6 +1447,9 @@ __device__ void softmax_wg(const DecodeParams& p, const WgCtx& w, const SegView<
             fence_before_sync();
             mbar_arrive(&w.bars[S_FREE + slot]);
 
+            // Causal mask.  A hidden token's weight is 0, and 0 * NaN would reach
+            // the rows that do not see it: a NaN row's channels are zeroed in the
+            // tile, where the rows that do see it have NaN weights anyway.
             if constexpr (E) {
                 const int tile_t0 = sg.t0 + it * kTT;
                 if (tile_t0 + kTT > mask_from) {    // token tile_t0 + srow is hidden from rows
@@ -1450,6 +1457,12 @@ __device__ void softmax_wg(const DecodeParams& p, const WgCtx& w, const SegView<
 #pragma unroll
                     for (int j = 0; j < kHL; ++j)
                         if (t >= lim[w.hb + j]) s[j] = -INFINITY;
+                    if (nan_row) {                  // (its QK^T is done, its PV waits for P_FULL)
+                        uint8_t* v = w.base + kOffStage + (i % L::kStg) * kStage + w.srow * 128;
+#pragma unroll 1
+                        for (int c = 16 * (w.lane >> 4), n = 16; n > 0; --n, ++c)
+                            *reinterpret_cast<uint4*>(v + (c >> 3) * kBlk + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
                 }
             }
             bool need = false;

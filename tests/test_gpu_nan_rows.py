@@ -89,8 +89,22 @@ def test_the_lone_tokens_above_are_segments_of_their_own():
 @pytest.mark.parametrize("heads,lens,q_lens,hits", [
     (16, [1, 9], [1, 9], {0: [0]}),                             # 16 rows of one token to a block
     (1, [1, 40], [1, 3], {0: [0]}),
+    (1, [200], [40], {0: [199]}),                               # the last of 40 new tokens: the other 39 do not see it
+    (4, [200, 130], [40, 9], {0: [180, 199], 1: [125]}),
+    (16, [300, 70], [70, 70], {0: [299], 1: [0]}),
+    (2, [129, 64], [17, 64], {0: [128], 1: [33, 40]}),          # the NaN token starts a tile
     (128, [200], [3], {0: [199]}),                              # several blocks to a token: none hides a token from itself
+    (7, [2000], [30], {0: [1990]}),                             # blocks split over CTAs
     (16, [200, 64], [4, 4], {0: range(64)}),                    # a tile of NaN before the new tokens
+    (3, [700], [64], {0: range(660, 700, 3)}),
 ])
 def test_extend(heads, lens, q_lens, hits, part, dtype):
     _check(_workload(heads, lens, 3 if heads == 4 else 1, q_lens), hits, part, dtype)
+
+
+@pytest.mark.parametrize("dtype", POOLS)
+def test_extend_with_a_nan_query_row(dtype):
+    """A non-finite query row does not make the tokens that others see pass for NaN rows."""
+    _check(_workload(4, [200], 1, [40]), {0: [199]}, "c_kv", dtype, nan_query=(3, 1))
+    _check(_workload(1, [90], 1, [33]), {}, "c_kv", dtype, nan_query=(0, 0))
+    _check(_workload(1, [90], 1, [33]), {0: [89]}, "c_kv", dtype, nan_query=(0, 0))
