@@ -451,7 +451,7 @@ mla_merge_kernel(const int32_t* __restrict__ merge, int n_merge, int part_rows,
         }
         m = mc;
     }
-    const float inv = 1.f / wsum;
+    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;   // 0: no partial saw a token (all outside the pool), an empty context
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     if (t == 0) lse[row] = m + logf(wsum);
 }
