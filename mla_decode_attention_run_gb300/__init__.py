@@ -194,12 +194,36 @@ def _device(where: str, t) -> int:
     raise ValueError(f"{where}: a tensor is not on the current CUDA device")
 
 
+def _check_pools(where: str, plan, ckv_pool, kpe_pool, slots: int):
+    """Refuses pools that cannot be of the plan's type: rows narrower than the
+    kernels read (a 4-bit pool on another plan), and on a 4-bit plan typed
+    8-bit or wider elements, fewer rows than slots, another device.  (Strides
+    are checked by the library.  Byte pools as such do not tell whether they
+    hold E4M3 or 4-bit rows.)  Returns the device where it was looked up."""
+    if plan.kv_dtype != MLA_KV_FP4_E2M1:
+        if ckv_pool.size(-1) < D_CKV or kpe_pool.size(-1) < D_KPE:
+            raise ValueError(f"{where}: pool rows of {ckv_pool.size(-1)} and {kpe_pool.size(-1)} channels, "
+                             f"not {D_CKV} and {D_KPE} (a 4-bit pool needs a 4-bit plan)")
+        return None
+    if ckv_pool.element_size() != 1 or kpe_pool.element_size() != 1 or (
+            ckv_pool.is_floating_point() or kpe_pool.is_floating_point()):
+        raise TypeError(f"{where}: pools of dtypes {ckv_pool.dtype} and {kpe_pool.dtype}; a 4-bit plan reads byte rows")
+    dev = _device(where, ckv_pool)
+    (n, width), (n_pe, width_pe) = ckv_pool.shape, kpe_pool.shape
+    if n < slots or n_pe < slots or width < FP4_CKV_BYTES <= ckv_pool.stride(0) or (
+            width_pe < FP4_KPE_BYTES <= kpe_pool.stride(0)) or kpe_pool.get_device() != dev:
+        raise ValueError(f"{where}: pools are not {slots} or more rows of {FP4_CKV_BYTES} and {FP4_KPE_BYTES} or more bytes "
+                         f"on one device (shapes {(n, width)}, {(n_pe, width_pe)})")
+    return dev
+
+
 class Plan:
     """Owns a plan handle; destroyed explicitly or when garbage collected."""
 
     def __init__(self):
         self.handle = _P(None)
         self.workspace_bytes = 0
+        self.kv_dtype = MLA_KV_FP8_E4M3      # what its pools hold
 
     def __del__(self):
         try:
@@ -221,6 +245,7 @@ def mla_decode_plan(kv_indptr_host, seq_lens_host, batch: int, num_heads: int, p
                                batch, num_heads, page_size, kv_dtype, ctypes.byref(ws),
                                _stream(stream)), "mla_decode_plan")
     plan.workspace_bytes = ws.value
+    plan.kv_dtype = kv_dtype
     plan._keep = (indptr, lens)          # host arrays live until the upload is done
     return plan
 
@@ -229,16 +254,19 @@ def mla_decode_run(plan: Plan, q, ckv_pool, kpe_pool, num_pool_slots: int, kv_in
                    kv_indices_dev, seq_lens_dev, k_scale: float, softmax_scale: float, out, lse,
                    workspace=None, stream=None):
     """q: bf16 [B, H, 576] (any strides with contiguous last dim); pools:
-    uint8 / float8 (FP8 plans) or bf16 (BF16 plans) with rows along dim 0;
+    uint8 / float8 (FP8 plans), bf16 (BF16 plans) or uint8 (4-bit plans) with
+    rows along dim 0, at least 512 and 64 channels wide (4-bit plans:
+    FP4_CKV_BYTES and FP4_KPE_BYTES bytes);
     out: bf16 [B, H, 512]; lse: fp32 [B, H]; workspace: >= plan.workspace_bytes."""
     lib = library()
+    dev = _check_pools("mla_decode_run", plan, ckv_pool, kpe_pool, num_pool_slots)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib.mla_decode_run(plan.handle, q.data_ptr(), q.stride(0), q.stride(1),
                               ckv_pool.data_ptr(), _row_stride_bytes(ckv_pool),
                               kpe_pool.data_ptr(), _row_stride_bytes(kpe_pool), num_pool_slots,
                               kv_indptr_dev.data_ptr(), _dptr(kv_indices_dev),
                               seq_lens_dev.data_ptr(), k_scale, softmax_scale, out.data_ptr(),
-                              lse.data_ptr(), _dptr(workspace), ws_bytes, _stream(stream)),
+                              lse.data_ptr(), _dptr(workspace), ws_bytes, _stream(stream, dev)),
            "mla_decode_run")
 
 
@@ -250,12 +278,13 @@ def mla_decode_run_static_scratch(plan: Plan, q, ckv_pool, kpe_pool, num_pool_sl
     the library (STATIC_SCRATCH_BYTES per GPU, kept until exit).  Calls that
     overlap on the GPU share that array and race; calls on one stream are
     ordered.  Raises MLAError (status 3) if the plan needs more scratch."""
+    dev = _check_pools("mla_decode_run_static_scratch", plan, ckv_pool, kpe_pool, num_pool_slots)
     _check(library().mla_decode_run_static_scratch(
         plan.handle, q.data_ptr(), q.stride(0), q.stride(1), ckv_pool.data_ptr(),
         _row_stride_bytes(ckv_pool), kpe_pool.data_ptr(), _row_stride_bytes(kpe_pool),
         num_pool_slots, kv_indptr_dev.data_ptr(), _dptr(kv_indices_dev),
         seq_lens_dev.data_ptr(), k_scale, softmax_scale, out.data_ptr(), lse.data_ptr(),
-        _stream(stream)), "mla_decode_run_static_scratch")
+        _stream(stream, dev)), "mla_decode_run_static_scratch")
 
 
 def mla_decode_plan_destroy(plan: Plan):
@@ -304,6 +333,7 @@ def mla_extend_plan(qo_indptr_host, kv_indptr_host, seq_lens_host, batch: int, n
                                lens.ctypes.data, batch, num_heads, page_size, kv_dtype,
                                ctypes.byref(ws), _stream(stream)), "mla_extend_plan")
     plan.workspace_bytes = ws.value
+    plan.kv_dtype = kv_dtype
     plan._keep = (qo, indptr, lens)
     return plan
 
@@ -313,6 +343,7 @@ def mla_extend_run(plan: Plan, q, ckv_pool, kpe_pool, num_pool_slots: int, kv_in
                    workspace=None, stream=None):
     """q: bf16 [n_q, H, 576] (contiguous last dim); out: bf16 [n_q, H, 512];
     lse: fp32 [n_q, H]; the rest as mla_decode_run."""
+    dev = _check_pools("mla_extend_run", plan, ckv_pool, kpe_pool, num_pool_slots)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(library().mla_extend_run(plan.handle, q.data_ptr(), q.stride(0), q.stride(1),
                                     ckv_pool.data_ptr(), _row_stride_bytes(ckv_pool),
@@ -320,7 +351,7 @@ def mla_extend_run(plan: Plan, q, ckv_pool, kpe_pool, num_pool_slots: int, kv_in
                                     num_pool_slots, kv_indptr_dev.data_ptr(),
                                     _dptr(kv_indices_dev), seq_lens_dev.data_ptr(), k_scale,
                                     softmax_scale, out.data_ptr(), lse.data_ptr(),
-                                    _dptr(workspace), ws_bytes, _stream(stream)),
+                                    _dptr(workspace), ws_bytes, _stream(stream, dev)),
            "mla_extend_run")
 
 
