@@ -1862,7 +1862,9 @@ __global__ void __maxnreg__((Roles<G, F4>::kRegs))
         w.row = quad * 32 + lane;
         w.srow = quad * 16 + (lane & 15);
         w.wg = G == 16 ? 0 : (warp - R::kWarpWg) >> 2;
-        w.wq = (warp - R::kWarpWg) & 3;
+        // (16 heads: the quadrants' sums are added in the same order for both
+        // pool types, from the third on, although the warps' numbers differ)
+        w.wq = G == 16 ? (quad + 2) & 3 : quad;
         w.h0 = 16 * w.wg;
         w.hb = w.h0 + (lane >> 4) * 8;
         w.lane = lane;
