@@ -325,8 +325,8 @@ mla_status_t mla_decode_plan_info(mla_plan_t plan, int32_t* num_ctas,
  * into segments_out (may be NULL), in launch order; tile_tokens receives the
  * kernel's tile (segments start on tile boundaries) and kernel the decode
  * kernel the plan would launch: 0 = mma.sync (BF16 pools), 1 = tcgen05 on
- * the E4M3 bytes (FP8 pools; 16 heads per CTA, 32 when H is a multiple of
- * 32, more heads as more CTAs).  The
+ * E4M3 bytes (FP8 and 4-bit pools; 16 heads per CTA, 32 when H is a multiple
+ * of 32, more heads as more CTAs).  The
  * mma.sync schedule gives each CTA an equal share of tiles; the tcgen05 one
  * balances tiles plus a fixed cost per segment.  Validates exactly like
  * mla_decode_plan.  Output pointers may be NULL.

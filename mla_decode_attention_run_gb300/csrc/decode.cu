@@ -8,6 +8,9 @@
 // Gather-Then-Cast Pivot", section "The Subject Message"), and the 576 =
 // 512 + 64 row split comes from "The KV Cache Cast Bottleneck", "The Context".
 //
+// E4M3 and 4-bit pools run in decode_tc.cu; the mma.sync kernel here reads BF16
+// pools (the cast-then-attend baselines).
+//
 // Kernel design (one CTA = one token range x 16 heads, 4 warps):
 //  * the 16 heads share every KV row (MLA: one latent KV head), so a CTA
 //    loads each gathered row once for all 16 heads: QK^T is a [16 x 576] x
@@ -15,9 +18,6 @@
 //    tensor cores (mma.sync m16n8k16, fp32 accumulate);
 //  * rows are gathered with 16-byte cp.async (zero fill for masked rows) into
 //    a two-stage ring, slot indices prefetched one tile ahead;
-//  * E4M3 rows are widened to f16 in shared memory (exact: E4M3 is a subset
-//    of f16); q is brought to f16 with a per-head power-of-two scale, so the
-//    product is exact and the scale folds into the score multiplier;
 //  * online softmax in the log2 domain; warps split QK^T by tokens and PV by
 //    output channels (128 each), exchanging the tile max and P through smem;
 //  * split-KV: segments of a request spread over CTAs write fp32 partials
@@ -39,21 +39,17 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kRow16 = kDQk + 8;     // padded 16-bit row (584 elements = 1168 B)
 constexpr int kPRow = kT + 8;        // padded P row (72 elements)
 
-template <bool kFp8>
 struct Smem {
-    static constexpr int kRawRow = kFp8 ? kDQk : kRow16 * 2;              // bytes
+    static constexpr int kRawRow = kRow16 * 2;                            // bytes
     static constexpr size_t kQ = 0;
     static constexpr size_t kRaw = kQ + size_t(kHeadsPerCta) * kRow16 * 2;
-    static constexpr size_t kKv = kRaw + size_t(2) * kT * kRawRow;        // FP8 only
-    static constexpr size_t kP = kKv + (kFp8 ? size_t(kT) * kRow16 * 2 : 0);
+    static constexpr size_t kP = kRaw + size_t(2) * kT * kRawRow;
     static constexpr size_t kRed = kP + size_t(kHeadsPerCta) * kPRow * 2;
     static constexpr size_t kL = kRed + size_t(kWarps) * kHeadsPerCta * 4;
     static constexpr size_t kCoef = kL + size_t(kWarps) * kHeadsPerCta * 4;
     static constexpr size_t kMask = kCoef + size_t(kHeadsPerCta) * 4;   // 4 tiles x 64 rows
     static constexpr size_t kBytes = kMask + size_t(4) * kT;
 };
-
-
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -75,43 +71,33 @@ __device__ __forceinline__ int64_t fetch_slot(const DecodeParams& p, const int32
 
 // Gather the 16 rows of this warp (rows warp + 4k) into a raw stage and
 // record which rows hold a real token (mask ring slot for this tile).
-template <bool kFp8>
 __device__ __forceinline__ void issue_rows(const DecodeParams& p, uint8_t* stage, int64_t slot_reg,
                                            uint8_t* mask, int warp, int lane) {
-    using S = Smem<kFp8>;
     if (lane < 16) mask[warp + 4 * lane] = slot_reg >= 0 ? 1 : 0;
 #pragma unroll 4
     for (int k = 0; k < 16; ++k) {
         const int64_t s = __shfl_sync(0xffffffffu, slot_reg, k);
         const uint32_t n = s >= 0 ? 16u : 0u;
         const int64_t ss = s >= 0 ? s : 0;
-        uint8_t* dst = stage + (warp + 4 * k) * S::kRawRow;
+        uint8_t* dst = stage + (warp + 4 * k) * Smem::kRawRow;
         const uint8_t* ck = p.ckv + ss * p.ckv_stride;
         const uint8_t* kp = p.kpe + ss * p.kpe_stride;
-        if constexpr (kFp8) {
-            cp_async16(dst + 16 * lane, ck + 16 * lane, n);                  // 512 B c_kv
-            if (lane < 4) cp_async16(dst + 512 + 16 * lane, kp + 16 * lane, n);  // 64 B k_pe
-        } else {
-            cp_async16(dst + 16 * lane, ck + 16 * lane, n);                  // 1024 B c_kv
-            cp_async16(dst + 512 + 16 * lane, ck + 512 + 16 * lane, n);
-            if (lane < 8) cp_async16(dst + 1024 + 16 * lane, kp + 16 * lane, n);  // 128 B k_pe
-        }
+        cp_async16(dst + 16 * lane, ck + 16 * lane, n);                  // 1024 B c_kv
+        cp_async16(dst + 512 + 16 * lane, ck + 512 + 16 * lane, n);
+        if (lane < 8) cp_async16(dst + 1024 + 16 * lane, kp + 16 * lane, n);  // 128 B k_pe
     }
     cp_async_commit();
 }
 
-template <bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1) mla_decode_mma_kernel(const DecodeParams p) {
-    using S = Smem<kFp8>;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint16_t* sQ = reinterpret_cast<uint16_t*>(smem + S::kQ);
-    uint8_t* sRaw = smem + S::kRaw;
-    uint16_t* sKvF16 = reinterpret_cast<uint16_t*>(smem + S::kKv);
-    uint16_t* sP = reinterpret_cast<uint16_t*>(smem + S::kP);
-    float* sRed = reinterpret_cast<float*>(smem + S::kRed);
-    float* sL = reinterpret_cast<float*>(smem + S::kL);
-    float* sCoef = reinterpret_cast<float*>(smem + S::kCoef);
-    uint8_t* sMask = smem + S::kMask;
+    uint16_t* sQ = reinterpret_cast<uint16_t*>(smem + Smem::kQ);
+    uint8_t* sRaw = smem + Smem::kRaw;
+    uint16_t* sP = reinterpret_cast<uint16_t*>(smem + Smem::kP);
+    float* sRed = reinterpret_cast<float*>(smem + Smem::kRed);
+    float* sL = reinterpret_cast<float*>(smem + Smem::kL);
+    float* sCoef = reinterpret_cast<float*>(smem + Smem::kCoef);
+    uint8_t* sMask = smem + Smem::kMask;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, j = lane & 3;
@@ -130,9 +116,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_mma_kernel(const Decod
 
         // start the KV gather before touching q
         int64_t slot_next = fetch_slot(p, pages, t0, t1, warp, lane);
-        issue_rows<kFp8>(p, sRaw, slot_next, sMask, warp, lane);
+        issue_rows(p, sRaw, slot_next, sMask, warp, lane);
         slot_next = fetch_slot(p, pages, t0 + kT, t1, warp, lane);
-        issue_rows<kFp8>(p, sRaw + kT * S::kRawRow, slot_next, sMask + kT, warp, lane);
+        issue_rows(p, sRaw + kT * Smem::kRawRow, slot_next, sMask + kT, warp, lane);
         slot_next = fetch_slot(p, pages, t0 + 2 * kT, t1, warp, lane);
 
         // ---- q rows of this head group -> sQ (16-bit), score multipliers
@@ -140,47 +126,18 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_mma_kernel(const Decod
             const int head = head0 + r;
             const bool valid = head < p.heads;
             const uint4* src = reinterpret_cast<const uint4*>(p.q + b * p.q_sb + head * p.q_sh);
-            uint4 v[3];
-            float amax = 0.f;
+            uint4 v[3];                              // all loads before the stores
 #pragma unroll
             for (int c = 0; c < 3; ++c) {
                 const int idx = lane + 32 * c;
                 v[c] = (valid && idx < kDQk / 8) ? src[idx] : make_uint4(0, 0, 0, 0);
-                const uint32_t w4[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    amax = fmaxf(amax, fabsf(__uint_as_float(w4[e] << 16)));
-                    amax = fmaxf(amax, fabsf(__uint_as_float(w4[e] & 0xffff0000u)));
-                }
-            }
-            float coef = valid ? p.softmax_scale * p.k_scale * kLog2e : 0.f;
-            float qscale = 1.f;
-            if constexpr (kFp8) {
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                int e = 0;
-                frexpf(amax, &e);                    // amax = m * 2^e, m in [0.5, 1)
-                int sigma = amax > 0.f ? 15 - e : 0; // max |q| * 2^sigma in [2^14, 2^15)
-                sigma = sigma > 100 ? 100 : (sigma < -100 ? -100 : sigma);
-                qscale = ldexpf(1.f, sigma);
-                coef = ldexpf(coef, -sigma);
             }
 #pragma unroll
             for (int c = 0; c < 3; ++c) {
                 const int idx = lane + 32 * c;
-                if (idx >= kDQk / 8) continue;
-                uint4 o = v[c];
-                if constexpr (kFp8) {
-                    const uint32_t w4[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-                    uint32_t h4[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        h4[e] = pack_f16x2(__uint_as_float(w4[e] << 16) * qscale,
-                                           __uint_as_float(w4[e] & 0xffff0000u) * qscale);
-                    o = make_uint4(h4[0], h4[1], h4[2], h4[3]);
-                }
-                *reinterpret_cast<uint4*>(sQ + r * kRow16 + idx * 8) = o;
+                if (idx < kDQk / 8) *reinterpret_cast<uint4*>(sQ + r * kRow16 + idx * 8) = v[c];
             }
+            const float coef = valid ? p.softmax_scale * p.k_scale * kLog2e : 0.f;
             if (lane == 0) sCoef[r] = coef;
         }
         // (sQ / sCoef become visible at the first barrier of the tile loop)
@@ -192,36 +149,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_mma_kernel(const Decod
 
         for (int it = 0; it < n_tiles; ++it) {
             const int stage = it & 1;
-            uint8_t* raw = sRaw + stage * kT * S::kRawRow;
+            uint8_t* raw = sRaw + stage * kT * Smem::kRawRow;
             cp_async_wait<1>();
             __syncthreads();                                         // (A) tile `it` landed
-            const uint16_t* kv;
-            if constexpr (kFp8) {
-                // widen E4M3 -> f16: 16 bytes in, 32 bytes out per step
-                for (int c = tid; c < kT * (kDQk / 16); c += kThreads) {
-                    const int row = c / (kDQk / 16), col = c % (kDQk / 16);
-                    const uint4 in = *reinterpret_cast<const uint4*>(raw + row * kDQk + col * 16);
-                    const uint32_t w4[4] = {in.x, in.y, in.z, in.w};
-                    uint32_t h[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        h[2 * e] = e4m3x2_to_f16x2(static_cast<uint16_t>(w4[e] & 0xffffu));
-                        h[2 * e + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w4[e] >> 16));
-                    }
-                    uint4* d = reinterpret_cast<uint4*>(sKvF16 + row * kRow16 + col * 16);
-                    d[0] = make_uint4(h[0], h[1], h[2], h[3]);
-                    d[1] = make_uint4(h[4], h[5], h[6], h[7]);
-                }
-                __syncthreads();                                     // (B) f16 tile ready
-                if (it + 2 < n_tiles)
-                    issue_rows<kFp8>(p, raw, slot_next, sMask + ((it + 2) & 3) * kT, warp, lane);
-                else
-                    cp_async_commit();
-                slot_next = fetch_slot(p, pages, t0 + (it + 3) * kT, t1, warp, lane);
-                kv = sKvF16;
-            } else {
-                kv = reinterpret_cast<const uint16_t*>(raw);
-            }
+            const uint16_t* kv = reinterpret_cast<const uint16_t*>(raw);
 
             // ---- S = Q K^T for this warp's 16 tokens (2 n-tiles of 8)
             float sacc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -233,8 +164,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_mma_kernel(const Decod
                 uint32_t a[4], b0, b1, b2, b3;
                 ldmatrix_x4(a[0], a[1], a[2], a[3], qrow + kb * 16);
                 ldmatrix_x4(b0, b1, b2, b3, krow + kb * 16);
-                mma_16816<!kFp8>(sacc[0], a, b0, b1);
-                mma_16816<!kFp8>(sacc[1], a, b2, b3);
+                mma_16816(sacc[0], a, b0, b1);
+                mma_16816(sacc[1], a, b2, b3);
             }
 
             // ---- online softmax (log2 domain)
@@ -283,9 +214,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_mma_kernel(const Decod
                 ps_hi += p2 + p3;
                 const int col = 16 * warp + 8 * nt + 2 * j;
                 *reinterpret_cast<uint32_t*>(sP + g * kPRow + col) =
-                    kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+                    pack_bf16x2(p0, p1);
                 *reinterpret_cast<uint32_t*>(sP + (g + 8) * kPRow + col) =
-                    kFp8 ? pack_f16x2(p2, p3) : pack_bf16x2(p2, p3);
+                    pack_bf16x2(p2, p3);
             }
             l_lo = l_lo * al_lo + ps_lo;
             l_hi = l_hi * al_hi + ps_hi;
@@ -310,18 +241,16 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_mma_kernel(const Decod
                 for (int np = 0; np < 8; ++np) {
                     uint32_t b0, b1, b2, b3;
                     ldmatrix_x4_trans(b0, b1, b2, b3, vrow + 16 * np);
-                    mma_16816<!kFp8>(o_acc[2 * np], a, b0, b1);
-                    mma_16816<!kFp8>(o_acc[2 * np + 1], a, b2, b3);
+                    mma_16816(o_acc[2 * np], a, b0, b1);
+                    mma_16816(o_acc[2 * np + 1], a, b2, b3);
                 }
             }
-            if constexpr (!kFp8) {
-                __syncthreads();                                     // (E) raw stage free
-                if (it + 2 < n_tiles)
-                    issue_rows<kFp8>(p, raw, slot_next, sMask + ((it + 2) & 3) * kT, warp, lane);
-                else
-                    cp_async_commit();
-                slot_next = fetch_slot(p, pages, t0 + (it + 3) * kT, t1, warp, lane);
-            }
+            __syncthreads();                                         // (E) raw stage free
+            if (it + 2 < n_tiles)
+                issue_rows(p, raw, slot_next, sMask + ((it + 2) & 3) * kT, warp, lane);
+            else
+                cp_async_commit();
+            slot_next = fetch_slot(p, pages, t0 + (it + 3) * kT, t1, warp, lane);
         }
         cp_async_wait<0>();
 
@@ -342,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_mma_kernel(const Decod
             L_lo += sL[w * kHeadsPerCta + g];
             L_hi += sL[w * kHeadsPerCta + g + 8];
         }
-        const float vscale = p.k_scale;             // v_t = value * k_scale for both pool types
+        const float vscale = p.k_scale;             // v_t = value * k_scale
         const float inv_lo = L_lo > 0.f ? vscale / L_lo : 0.f;
         const float inv_hi = L_hi > 0.f ? vscale / L_hi : 0.f;
         const int h_lo = head0 + g, h_hi = head0 + g + 8;
@@ -457,21 +386,19 @@ mla_merge_kernel(const int32_t* __restrict__ merge, int n_merge, int part_rows,
 }
 
 std::mutex g_attr_mu;
-std::vector<int> g_attr_done;   // per device: bit0 fp8 kernel, bit1 bf16 kernel
+std::vector<char> g_attr_done;   // per device: max dynamic smem set
 
-template <bool kFp8>
 cudaError_t ensure_smem_attr() {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lk(g_attr_mu);
     if ((int)g_attr_done.size() <= dev) g_attr_done.resize(dev + 1, 0);
-    const int bit = kFp8 ? 1 : 2;
-    if (!(g_attr_done[dev] & bit)) {
-        e = cudaFuncSetAttribute(mla_decode_mma_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(Smem<kFp8>::kBytes));
+    if (!g_attr_done[dev]) {
+        e = cudaFuncSetAttribute(mla_decode_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(Smem::kBytes));
         if (e != cudaSuccess) return e;
-        g_attr_done[dev] |= bit;
+        g_attr_done[dev] = 1;
     }
     return cudaSuccess;
 }
@@ -511,7 +438,6 @@ mla_status_t run_plan(mla_plan_t plan, bool extend, const void* q, int64_t q_str
     }
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev != plan->device) return MLA_ERR_INVALID_ARG;
-    const bool fp8 = s.kv_dtype == MLA_KV_FP8_E4M3;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
 
     DecodeParams p;
@@ -559,16 +485,8 @@ mla_status_t run_plan(mla_plan_t plan, bool extend, const void* q, int64_t q_str
         if (launch_decode_tc(p, plan->ranges, s.num_ctas, fp4, cs) != cudaSuccess) return MLA_ERR_CUDA;
     } else if (s.num_ctas > 0) {
         const dim3 grid(s.num_ctas * s.head_groups);
-        cudaError_t e;
-        if (fp8) {
-            e = ensure_smem_attr<true>();
-            if (e != cudaSuccess) return MLA_ERR_CUDA;
-            mla_decode_mma_kernel<true><<<grid, kThreads, Smem<true>::kBytes, cs>>>(p);
-        } else {
-            e = ensure_smem_attr<false>();
-            if (e != cudaSuccess) return MLA_ERR_CUDA;
-            mla_decode_mma_kernel<false><<<grid, kThreads, Smem<false>::kBytes, cs>>>(p);
-        }
+        if (ensure_smem_attr() != cudaSuccess) return MLA_ERR_CUDA;
+        mla_decode_mma_kernel<<<grid, kThreads, Smem::kBytes, cs>>>(p);
         if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
     }
     if (s.n_merge() > 0) {

@@ -24,9 +24,9 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 // Resident decode CTAs per SM (both kernels' shared-memory budgets allow one).
 int ctas_per_sm(DecodeKernel) { return 1; }
 
-// The tcgen05 kernel covers FP8 and 4-bit pools (16 heads per CTA, more heads
-// as more CTAs); the mma.sync kernel BF16 pools.
-DecodeKernel pick_kernel(mla_kv_dtype_t dtype, int32_t) {
+// The tcgen05 kernel covers FP8 and 4-bit pools (16 or 32 heads per CTA, more
+// heads as more CTAs); the mma.sync kernel BF16 pools.
+DecodeKernel pick_kernel(mla_kv_dtype_t dtype) {
     return dtype == MLA_KV_BF16 ? DecodeKernel::kMma : DecodeKernel::kTc;
 }
 
@@ -200,7 +200,7 @@ mla_status_t build_schedule(const int32_t* indptr, const int32_t* seq, int32_t B
     const mla_status_t st = validate_plan_inputs(indptr, seq, B, H, ps, dtype);
     if (st != MLA_OK) return st;
     if (num_sms < 1) return MLA_ERR_INVALID_ARG;
-    const DecodeKernel kernel = pick_kernel(dtype, H);
+    const DecodeKernel kernel = pick_kernel(dtype);
     const int64_t tile = kernel == DecodeKernel::kTc ? kTcTileTokens : kTileTokens;
     int64_t n_tokens = 0, n_tiles = 0;
     for (int32_t b = 0; b < B; ++b) {

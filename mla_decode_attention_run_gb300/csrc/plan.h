@@ -30,8 +30,8 @@ constexpr int kTcQImageBytes = 3 * kHeadsPerCta * 576 + kHeadsPerCta * 12;
 
 // Which decode kernel a plan launches.
 enum class DecodeKernel : int32_t {
-    kMma = 0,   // mma.sync, E4M3 widened to f16 in smem; also the BF16-pool kernel
-    kTc = 1,    // tcgen05 kind::f8f6f4 on the E4M3 bytes in place (FP8, H <= 16)
+    kMma = 0,   // mma.sync: BF16 pools
+    kTc = 1,    // tcgen05 kind::f8f6f4: E4M3 pools in place, 4-bit pools widened to E4M3
 };
 
 // The split-KV schedule.  The concatenation of all requests' tiles is cut
