@@ -36,14 +36,6 @@
 // O accumulates in TMEM across a segment's tiles; when m does move, the
 // softmax warps rescale it in place before the next PV may add to it.
 //
-// Whether a segment's q image may be fetched as soon as the one before it has
-// had its last QK^T (q_fetch_fp4), not only after its epilogue: 4-bit pools'
-// 16-head CTAs (which have one image buffer) and 32-head extend (256-token
-// extend 657 vs 670 us on GB300); 32-head decode, whose segments are long, ran
-// 128 heads in 2.50 ms with it and 2.38 without.
-template <int G, bool E, bool F4>
-constexpr bool early_q() { return F4 && (E || G == 16); }
-
 // A CTA serves G = 16 or 32 heads of its token range (32 when H is a multiple
 // of 32); more heads run as more CTAs (grid.y = head group).  The groups of a
 // token range start together, so their repeated reads of the same rows
@@ -52,12 +44,15 @@ constexpr bool early_q() { return F4 && (E || G == 16); }
 // 4-bit pools (F4 = true; rows in fp4.cuh) run the same computation: a row's
 // values are E4M3 numbers, so the fill warps widen it, exactly, into the bytes
 // that an 8-bit pool's row would have, and everything behind the tile in shared
-// memory is the same.  What bounds a 16-head CTA there is the issue of
-// instructions and the L1 data pipe: a 64-token tile takes about 4,300 warp
-// instructions (8-bit 2,700), 1,850 of them widening, and 1,900 cycles, in which
-// a sub-partition issues 0.45 per cycle, half of them on the half-rate pipe of
-// permutes and logic, and the data pipe is busy two thirds of the time (batch-40
-// call 31.6 us on GB300, 8-bit 29.2).
+// memory is the same.  A 64-token tile of a 16-head CTA takes about 4,300 warp
+// instructions (8-bit 2,700), 1,850 of them widening, many of these on the
+// half-rate pipe of permutes and logic, and in a long run of tiles 1,740 cycles
+// (8-bit 1,350): a sub-partition then issues 0.6 per cycle, so the issue of
+// instructions is the nearest limit (batch-40 call 31.6 us on GB300, 8-bit 29.2).
+// With 32 rows a tile takes 5,600 (decode) to 6,300 (extend) warp instructions,
+// some 100 of them spills, and about 2,600 cycles (8-bit 3,700 to 4,000 and
+// 2,350): issue 0.54 to 0.61, the shared-memory pipe 54 to 59 % and the tensor
+// pipe 41 % busy, and no unit full.
 //
 // Extend (several new tokens per request, causal) is the same kernel built
 // with E = true: a CTA then serves a block of G query rows (token x head) of
@@ -65,7 +60,8 @@ constexpr bool early_q() { return F4 && (E || G == 16); }
 // at or past a row's limit on the tiles that reach them.
 //
 // Warp roles (one CTA per SM, persistent over its token range; warp numbers
-// for G = 16, 384 threads, with G = 32's in brackets, 512 threads):
+// for G = 16, 384 threads, with G = 32's in brackets, 512 threads; 4-bit pools
+// below):
 //   warp 11 [7]  publishes tiles ahead of the stage fills: resolves each row's
 //              pool slot (or -1: past the context, outside the pool) into a
 //              small shared ring and has L2 prefetch the rows' cache lines,
@@ -91,6 +87,10 @@ constexpr bool early_q() { return F4 && (E || G == 16); }
 //              heads, 16-31 the other 8), rescaling its heads' O columns when
 //              their maximum moves, and the epilogue (all lanes: lane = output
 //              channel).
+// 4-bit pools (512 threads at G = 16, 640 at G = 32): warps 0-3 and 4-7 copy
+// and widen the even and the odd tiles; 8 issues the QK^T MMAs, 9 fetches the
+// images, 10 issues the PV MMAs, 11 publishes the slots; 12-15 [and 16-19] are
+// the softmax warpgroups.
 // Every mbarrier wait is bounded; on a timeout the CTA sets
 // MLA_FLAG_WAIT_TIMEOUT, drains its MMAs and copies, frees TMEM and exits.
 // The 16-head and 32-head instantiations differ in several of these forms
@@ -183,9 +183,9 @@ struct Shape {
 // takes two warps per SM sub-partition to keep up with the softmax; they work
 // in two sets of kPer warps, on even and on odd tiles, so that a set's waits
 // (for slots, copies, a free stage) overlap the other's work.  A 32-head CTA
-// then has 640 threads at 96 registers (128-head call 2.43 ms on GB300,
-// against 2.84 with 512 threads at 128 registers and four fill warps, although
-// the softmax spills 72 bytes more).
+// then has 640 threads at 96 registers (when this was chosen the 128-head call
+// took 2.43 ms on GB300 with it, 2.84 with 512 threads at 128 registers and
+// four fill warps, although the softmax spills 72 bytes more; now 2.25).
 template <int G, bool F4>
 struct Roles {
     static constexpr int kFill = F4 ? 8 : kFillWarps;
@@ -197,6 +197,14 @@ struct Roles {
     static constexpr int kThreads = G == 16 && !F4 ? 384 : (G == 32 && F4 ? 640 : 512);
     static constexpr int kRegs = kThreads == 384 ? 152 : (kThreads == 640 ? 96 : 128);
 };
+
+// Whether a segment's q image may be fetched as soon as the one before it has
+// had its last QK^T (q_fetch_fp4), not only after its epilogue: 4-bit pools'
+// 16-head CTAs (which have one image buffer) and 32-head extend (8 x 256-token
+// extend 657 vs 670 us on GB300); 32-head decode, whose segments are long, ran
+// 128 heads in 2.50 ms with it and 2.38 without (2.25 as it stands now).
+template <int G, bool E, bool F4>
+constexpr bool early_q() { return F4 && (E || G == 16); }
 
 // shared memory map (offsets from a 1024-byte aligned base), the same for
 // both head counts
@@ -575,8 +583,8 @@ __device__ void fill_warp(const DecodeParams& p, uint8_t* base, uint64_t* bars, 
 // them from there to E4M3 (fp4.cuh) where cp.async puts an 8-bit pool's bytes.
 // Its next tile's copies go out as soon as the buffer is widened and land while
 // the other set works.  Other forms measured on GB300, batch-40 decode and
-// 256-token extend (this one 31.6 and 657 us): rows loaded into registers and
-// widened from there 41.2 and 934 us; four warps that only copy and four that
+// 8 x 256-token extend (this one 31.6 and 657 us then, 31.6 and 651 now): rows
+// loaded into registers and widened from there 41.2 and 934 us; four warps that only copy and four that
 // only widen 34.2 and 907; one set of eight warps, half a tile's rows each,
 // 36.1 and 887; one bulk copy per row from the scheduler 64 and 1348 (a bulk
 // copy of a row takes about 90 cycles to issue).
@@ -642,10 +650,10 @@ __device__ __forceinline__ void widen_store(uint8_t* lo, uint8_t* hi, const uint
 // Widens share w of a tile into its stage.
 // Two forms: 32 channels a step in a rolled loop whose next reads go out
 // before a step's stores (extend), or four steps' reads, then their stores
-// (decode).  Measured on GB300, rolled against grouped: 256-token extend 682
-// vs 804 us and 4-token extend 70.2 vs 77.9, where the larger body evicts the
-// other roles' code; batch-40 decode 33.4 vs 32.2 us, 128-head call 2.39 vs
-// 2.36 ms.
+// (decode).  Measured on GB300 when it was chosen, rolled against grouped: 8 x
+// 256-token extend 682 vs 804 us and 4-token extend 70.2 vs 77.9, where the
+// larger body evicts the other roles' code; batch-40 decode 33.4 vs 32.2 us,
+// 128-head call 2.39 vs 2.36 ms.
 template <int kPer, bool kRolled>
 __device__ __forceinline__ void widen_raw(uint8_t* stage, const uint8_t* raw, uint32_t tables, int w, int lane) {
     constexpr int kRows = RawPiece<kPer>::kRows, kSteps = kRows / 2;
@@ -852,7 +860,7 @@ __device__ void scheduler_fp4(const DecodeParams& p, uint8_t* base, uint64_t* ba
         // from DRAM and tiles pass quickly: 16-head decode (batch-40 call on rows
         // that are not in L2 35.1 vs 37.0 us on GB300).  32-head decode and extend
         // do better without the instructions (128-head call 2.27 vs 2.39 ms,
-        // 256-token extend 518 vs 523 us).
+        // extend of eight chunks of 82 to 256 tokens 518 vs 523 us).
         if constexpr (G == 16 && !E) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -1259,7 +1267,7 @@ __device__ void q_fetch(const DecodeParams& p, uint8_t* base, uint64_t* bars, vo
                   1000000000ull);
 }
 
-// The same for 4-bit pools.  The image has one buffer, free once its segment's
+// The same where early_q.  The image has one buffer, free once its segment's
 // last QK^T is done, so that the next one's can start beside the epilogue; the
 // multipliers and limits, which the epilogue still reads, have four: QK^T of
 // the third segment from here waits for an S buffer that the softmax frees
@@ -1792,10 +1800,9 @@ __global__ void __maxnreg__((Roles<G, F4>::kRegs))
     if (tid == 0) {
         // KV_FULL: 32 cp.async arrivals from each fill warp (4-bit pools: one
         // arrival from each warp of the tile's set); KV_EMPTY, S_FULL,
-        // PV_DONE, Q_FULL: one commit or bulk-copy arrival; S_FREE, P_FULL,
-        // O_FREE: every softmax thread; Q_FREE: those and the QK commit (4-bit
-        // pools: the commit alone); DONE:
-        // both MMA threads; SL_EMPTY: the fill warps and the softmax warps
+        // PV_DONE, Q_FULL, QC_FULL: one commit or bulk-copy arrival; S_FREE,
+        // P_FULL, O_FREE: every softmax thread; Q_FREE: those and the QK commit
+        // (the commit alone where early_q); DONE: both MMA threads; SL_EMPTY: the fill warps and the softmax warps
         constexpr uint32_t kSm = 128 * S::kWgs;
         for (int b = 0; b < kStages; ++b) {
             mbar_init(&bars[KV_FULL + b], F4 ? R::kPer : 32 * R::kFill);
