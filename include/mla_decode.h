@@ -138,8 +138,7 @@ mla_status_t mla_decode_plan(mla_plan_t* plan, const int32_t* kv_indptr_host,
  *     lse[b][h] = ln sum_t exp(s_t)               (fp32, natural log)
  * A request with seq_len 0 gets out = 0 and lse = -inf; a head whose query
  * row holds an infinity or a NaN gets out = NaN and lse = NaN, and so do all
- * heads of a request with a token whose cache row holds a NaN (FP8 and 4-bit
- * plans).
+ * heads of a request with a token whose cache row holds a NaN.
  * Arithmetic of FP8 plans: the E4M3 cache bytes are the tensor-core operands
  * as they are; each query row enters as three E4M3 terms (exactly for every
  * entry above 2^-14 of the row's largest, with 4 significant bits below) and

@@ -202,14 +202,18 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_mma_kernel(const Decod
                 t_hi = fmaxf(t_hi, sRed[w * kHeadsPerCta + g + 8]);
             }
             const float mn_lo = fmaxf(m_lo, t_lo), mn_hi = fmaxf(m_hi, t_hi);
-            const float al_lo = fast_exp2(m_lo - mn_lo), al_hi = fast_exp2(m_hi - mn_hi);
+            // the exponents' reference: any finite number while nothing has been
+            // seen (all tokens outside the pool, or NaN rows, whose scores move
+            // no maximum)
+            const float ref_lo = mn_lo == -INFINITY ? 0.f : mn_lo, ref_hi = mn_hi == -INFINITY ? 0.f : mn_hi;
+            const float al_lo = fast_exp2(m_lo - ref_lo), al_hi = fast_exp2(m_hi - ref_hi);
             m_lo = mn_lo;
             m_hi = mn_hi;
             float ps_lo = 0.f, ps_hi = 0.f;
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-                const float p0 = fast_exp2(s_lo[2 * nt] - mn_lo), p1 = fast_exp2(s_lo[2 * nt + 1] - mn_lo);
-                const float p2 = fast_exp2(s_hi[2 * nt] - mn_hi), p3 = fast_exp2(s_hi[2 * nt + 1] - mn_hi);
+                const float p0 = fast_exp2(s_lo[2 * nt] - ref_lo), p1 = fast_exp2(s_lo[2 * nt + 1] - ref_lo);
+                const float p2 = fast_exp2(s_hi[2 * nt] - ref_hi), p3 = fast_exp2(s_hi[2 * nt + 1] - ref_hi);
                 ps_lo += p0 + p1;
                 ps_hi += p2 + p3;
                 const int col = 16 * warp + 8 * nt + 2 * j;
@@ -272,8 +276,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_mma_kernel(const Decod
             L_hi += sL[w * kHeadsPerCta + g + 8];
         }
         const float vscale = p.k_scale;             // v_t = value * k_scale
-        const float inv_lo = L_lo > 0.f ? vscale / L_lo : 0.f;
-        const float inv_hi = L_hi > 0.f ? vscale / L_hi : 0.f;
+        const float inv_lo = L_lo == 0.f ? 0.f : vscale / L_lo;
+        const float inv_hi = L_hi == 0.f ? 0.f : vscale / L_hi;
         const int h_lo = head0 + g, h_hi = head0 + g + 8;
         const float lse_lo = (m_lo + log2f(L_lo)) * kLn2, lse_hi = (m_hi + log2f(L_hi)) * kLn2;
         if (part < 0) {
