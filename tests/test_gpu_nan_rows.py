@@ -97,6 +97,8 @@ def test_the_lone_tokens_above_are_segments_of_their_own():
     (7, [2000], [30], {0: [1990]}),                             # blocks split over CTAs
     (16, [200, 64], [4, 4], {0: range(64)}),                    # a tile of NaN before the new tokens
     (3, [700], [64], {0: range(660, 700, 3)}),
+    (1, [200], [9], {0: [199]}),                                # blocks of 16 rows (the others above: 32)
+    (4, [130, 3000], [3, 4], {0: [128], 1: [2998]}),
 ])
 def test_extend(heads, lens, q_lens, hits, part, dtype):
     _check(_workload(heads, lens, 3 if heads == 4 else 1, q_lens), hits, part, dtype)
